@@ -86,7 +86,11 @@ constexpr uint32_t kTmO = 2 * kTile, kTmOCols = 144;        // accumulators in t
 
 struct __align__(16) TcBars {
   int32_t ek[4][4], ev[2][4];   // exponents of the 32-token groups of a K / V tile
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], qfull[2], sfull[2], pfull[2], ofull[2], rfull;
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], qfull[2], sfull[2], pfull[2], ofull[2];
+  // The K unit's Rf has been staged; no softmax warp reads it any more. One phase each per staging, and
+  // every warp on both sides takes part in each: a wait is never more than one phase from what it is for,
+  // which is all that a parity tells apart.
+  uint64_t rfull, rfree;
   int32_t er;                   // exponent of the K unit's Rf
   int32_t pu[12][8];            // what a producer warp needs of its unit now and then
   uint32_t tmem;
@@ -898,7 +902,7 @@ struct Producer {
     asm volatile("bar.sync %0, %1;" ::"r"(isk ? 1 : 2), "n"(96 * SETS) : "memory");
     int it = 0;
     unit = -1;
-    if (lane == 0) pu[4] = 0, pu[6] = 0, pu[7] = 0;   // [6], [7]: segments of the two row tiles
+    if (lane == 0) pu[4] = 0, pu[6] = 0;   // [6]: Rf's staged
     __syncwarp();
     const int begin = blockIdx.x * a.seg;
   ChunkUnit u;
@@ -907,17 +911,11 @@ struct Producer {
       x = max(x, u.tile);
       if (x >= end) break;
       const int x1 = min(end, u.tile + u.tiles);
-      const int nq0 = pu[6], nq1 = pu[7];
-      __syncwarp();
-      if (lane == 0) {
-        pu[6] = nq0 + 1;
-        pu[7] = nq1 + (a.par == 1 || x1 - x > 1 ? 1 : 0);
-      }
       if (take(u.i, u.h, u.t)) {
-        if (isk) {   // the softmax groups have read the last unit's
-          if (nq0 > 0) tc_wait(bars, &bars->qfull[0], (nq0 - 1) & 1);
-          if (nq1 > 0) tc_wait(bars, &bars->qfull[1], (nq1 - 1) & 1);
-        }
+        const int staged = pu[6];
+        __syncwarp();
+        if (lane == 0) pu[6] = staged + 1;
+        if (isk && staged > 0) tc_wait(bars, &bars->rfree, (staged - 1) & 1);   // the softmax groups have read the last one
         stage_rf();
       }
       // the set's tiles: number x + skip on, every SETS-th
@@ -1137,11 +1135,10 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
     const int limit = real ? base + (a.kn ? tok + 1 : 0) : 0;
     const int plen = a.plen ? min(max(__ldg(a.plen + a.row[i]), 0), b0) : b0;
     const int first = par == 1 ? 0 : grp, step = par;   // tiles of this group
-    if (rank > 0 && unit != rf_unit) ++nrf, rf_unit = unit;   // the key producers stage every unit's Rf once
     int eq = 0;
+    // the row, and its products with Rf, into the operand tiles
+    const uint32_t qt = sb + kTcQ + grp * 32768, qx = sb + kTcQx + grp * 4096;
     if (first < n) {
-      // the row, and its products with Rf, into the operand tiles
-      const uint32_t qt = sb + kTcQ + grp * 32768, qx = sb + kTcQx + grp * 4096;
       if (any) {
         const int64_t at = (int64_t)(a.tok0[i] + (real ? tok : 0)) * a.qs + (u.h * a.hq + (real ? j : 0)) * 128;
         const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + at);
@@ -1186,7 +1183,13 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
           }
         }
       }
-      if (rank > 0) tc_wait(bars, &bars->rfull, (nrf - 1) & 1);
+    }
+    if (rank > 0 && unit != rf_unit) {   // the key producers stage every unit's Rf once; a group without tiles here waits too
+      tc_wait(bars, &bars->rfull, nrf & 1);
+      ++nrf;
+      rf_unit = unit;
+    }
+    if (first < n) {
       if (any && a.blk0_rank > 0) {
         if constexpr (SPLIT) meet();   // the whole query
         const float fr = pow2i(-*reinterpret_cast<volatile int32_t*>(&bars->er));
@@ -1218,6 +1221,10 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->qfull[grp]);
+    }
+    if (rank > 0 && u.t + 1 == chunk_blocks(a, i)) {   // the last segment that reads this Rf
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->rfree);
     }
     float mref = -INFINITY, l = 0.0f;
     int E = -120;
@@ -1510,6 +1517,7 @@ __device__ __forceinline__ void tc_begin(const ChunkArgs& a, TcBars* bars, int p
       mbar_init(&bars->ofull[s], 1);
     }
     mbar_init(&bars->rfull, stagers);
+    mbar_init(&bars->rfree, 2 * rows32);
     bars->dead = 0;
     bars->status = a.status;
     fence_mbarrier_init();
@@ -1574,7 +1582,7 @@ __device__ __forceinline__ void fetch_role(const ChunkArgs& a, TcBars* bars, uin
   const uint32_t sb = smem_u32(smem), rf = sb + kTcRf;
   uint64_t* full = isk ? bars->kfull : bars->vfull;
   uint64_t* empty = isk ? bars->kempty : bars->vempty;
-  int it = 0, segments = 0;
+  int it = 0, staged = 0;
   int64_t unit = -1;
   const int begin = blockIdx.x * a.seg;
   ChunkUnit u;
@@ -1585,17 +1593,14 @@ __device__ __forceinline__ void fetch_role(const ChunkArgs& a, TcBars* bars, uin
     const int x1 = min(end, u.tile + u.tiles);
     const int64_t now = (int64_t)a.row[u.i] * a.H + u.h;
     if (isk && now != unit && a.ncomp[u.i] > 0 && a.blk0_rank > 0) {
-      if (segments > 0) {   // the softmax groups have read the last unit's
-        tc_wait(bars, &bars->qfull[0], (segments - 1) & 1);
-        tc_wait(bars, &bars->qfull[1], (segments - 1) & 1);
-      }
+      if (staged > 0) tc_wait(bars, &bars->rfree, (staged - 1) & 1);   // the softmax groups have read the last one
+      ++staged;
       const int er = rf_to_smem(a.K.rfac + now * a.nblk_max * 128 * rp, rp, a.blk0_rank, rf, true);
       if (lane == 0) *reinterpret_cast<volatile int32_t*>(&bars->er) = er;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->rfull);
     }
     unit = now;
-    ++segments;
     if (lane == 0) {
       const uint8_t* src = a.img + (int64_t)(a.img0[u.i] + u.h * ((a.img0[u.i + 1] - a.img0[u.i]) / a.H) + x - u.tile) * kImgBytes;
       const uint32_t l_bytes = a.blk0_rank > 0 ? (isk ? kTile * 32 : kTcHalf) : 0;

@@ -138,3 +138,71 @@ def check_chunk(got, ref, bound, dt, what=""):
         rel = float(err.norm() / ref.norm())
         lim = max(1e-5, float(HALF[dt]) + 0.25 * float(bound.norm() / ref.norm()))
         assert rel <= lim, f"{what}: {rel:.2e} of the result's norm off, at most {lim:.2e}"
+
+
+def chunk_spread(kc, vc, rows, counts, q, kn, vn, tau, plen=None):
+    """(out, sigma), float64 [T][Hq][128] and [T][Hq]: the result, and the root mean square that the norm of a
+    row's error can have when its roundings are independent. A rounding to binary16 is at most 2^-11 of the
+    value off, d = 2^-11 / sqrt(3) in the root mean square. A key's or value's channel takes four of them at
+    most, each of no more than the sum `mag` of its parts (the scale's and the middle value's product, their
+    sum, a further one for a flushed block's low-rank part or an outlier's): its variance is below
+    (2 d mag)^2. So a score's is (2 d tau)^2 sum_c q_c^2 mag_c^2 =: e_t^2, which moves the result by
+    p_t e_t (V_t - out); the weight's own rounding moves it by p_t d V_t. Sums over tokens add the squares."""
+    d = 2.0 ** -11 / 3 ** 0.5
+    if kc.dtype == torch.float32:
+        d = 2.0 ** -24 * 128 ** 0.5   # a sum of 128 terms
+    Hq, H = q.shape[1], kc.c.H
+    hq = Hq // H
+    out = torch.zeros(q.shape, dtype=torch.float64, device=q.device)
+    var = torch.zeros(q.shape[:2], dtype=torch.float64, device=q.device)
+    at = 0
+    for b, n in zip(rows, counts):
+        if n == 0:
+            continue
+        (K, KM), (V, VM) = dense64(kc, b), dense64(vc, b)
+        base, b0 = K.shape[1], state(kc, b)[0]
+        if kn is not None:
+            k1, v1 = kn[at:at + n].double().transpose(0, 1), vn[at:at + n].double().transpose(0, 1)
+            K, KM, V, VM = (torch.cat(x, 1) for x in ((K, k1), (KM, k1.abs()), (V, v1), (VM, v1.abs())))
+        t = torch.arange(K.shape[1], device=q.device)
+        seen = t[None] < base + torch.arange(1, n + 1, device=q.device)[:, None]
+        if plen is not None:
+            p = min(max(int(plen[b]), 0), b0)
+            seen = seen & ~((t >= p) & (t < b0))[None]
+        live = seen.any(0)[:, None]
+        if K.shape[1] == 0:
+            at += n
+            continue
+        mask = seen.repeat_interleave(hq, 0)   # row (token, query head of the group)
+        for h in range(H):
+            k, km, v, vm = (torch.where(live, x[h], 0.0) for x in (K, KM, V, VM))
+            qq = q[at:at + n, h * hq:(h + 1) * hq].double().reshape(n * hq, 128)
+            S = (qq @ k.T * tau).masked_fill(~mask, -torch.inf)
+            m = S.amax(1, keepdim=True)
+            w = torch.where(mask, torch.exp(S - torch.where(m.isinf(), 0.0, m)), 0.0)
+            l = w.sum(1, keepdim=True)
+            w = torch.where(l > 0, w / l, 0.0)
+            o = w @ v
+            e2 = (2 * d * tau) ** 2 * (qq.square() @ km.square().T)
+            far = (v.square().sum(1)[None] - 2 * o @ v.T + o.square().sum(1, keepdim=True)).clamp_min(0)
+            s2 = (w.square() * (e2 * far + d * d * (v.square() + 4 * vm.square()).sum(1)[None])).sum(1)
+            out[at:at + n, h * hq:(h + 1) * hq] = o.view(n, hq, 128)
+            var[at:at + n, h * hq:(h + 1) * hq] = s2.view(n, hq)
+        at += n
+    return out, var.sqrt()
+
+
+def check_spread(got, ref, sigma, dt, what=""):
+    """Each row's error within 5 sigma of its norm (a row that one token dominates is nearly a single rounding,
+    at most sqrt(3) times its root mean square; the others are sums of many), all rows' together within twice
+    theirs, beside the output's own rounding, at most half a step of every element."""
+    assert not torch.isnan(got).any(), f"{what}: NaN"
+    err, size = (got.double() - ref).norm(dim=-1), HALF[dt] * ref.norm(dim=-1)
+    if dt == torch.float16:
+        size = size + 2.0 ** -25 * 128 ** 0.5   # results below 2^-14
+    floor = 1e-6 * ref.norm(dim=-1)             # binary32 sums of the result
+    bad = err > 5 * sigma + size + floor
+    worst = float((err / (5 * sigma + size + floor).clamp_min(1e-300)).max()) if err.numel() else 0.0
+    assert not bad.any(), f"{what}: {int(bad.sum())} rows off, {worst:.2f} times the limit, first {bad.nonzero()[0].tolist()}"
+    both = float(err.norm()), float(2 * sigma.norm() + size.norm() + floor.norm())
+    assert both[0] <= both[1], f"{what}: {both[0]:.3e} off in all, at most {both[1]:.3e}"
