@@ -35,7 +35,9 @@
 // accumulators of 128 + 16; with tiles of 128 the extra 16 would not fit its 512.
 //
 // The softmax reference of a row moves only when a tile's maximum passes it by
-// 2^8, so that the accumulator in tensor memory is rarely rescaled. Rounding to
+// 2^8, so that the accumulator in tensor memory is rarely rescaled. Weights are
+// 2^7 times the formula's (their sum too): with 2^8 above the reference they stay
+// below 2^15, and down to 2^-21 of it they keep binary16's 11 bits. Rounding to
 // binary16 happens to K and V (to the scale, the middle value and the sum of a code;
 // 11 bits against the codes' 2 to 8), to q Rf and L, and to the weights: the tensor
 // cores take no wider operands at this rate, and an output's error (1e-3 of its norm
@@ -83,6 +85,7 @@ constexpr uint32_t kImgV = 2 * kTcHalf + kTile * 32, kImgE = kImgV + 3 * kTcHalf
 static_assert(kImgE + 32 <= kImgBytes && kImgBytes % 128 == 0, "layout of a rebuilt tile");
 constexpr uint32_t kImgSmem = kImgE + 2 * kTcRfBytes + 256 + 1024;
 constexpr uint32_t kTmO = 2 * kTile, kTmOCols = 144;        // accumulators in tensor memory
+constexpr float kWeightShift = 7.0f;                        // log2 of what weights are multiplied by
 
 struct __align__(16) TcBars {
   int32_t ek[4][4], ev[2][4];   // exponents of the 32-token groups of a K / V tile
@@ -158,11 +161,22 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // 2^e, e clamped to binary32's normal range
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
 
-// Exponent of the power of two that values of at most `m` are divided by: none in
+__device__ __forceinline__ int exp_of(float m) { return (int)((__float_as_uint(m) >> 23) & 255) - 127; }
+
+// Exponent of the power of two that a query or an Rf of at most `m` is divided by: none in
 // [2^-6, 2^12), else one that puts m at 2^4.
 __device__ __forceinline__ int range_exp(float m) {
-  const int e = (int)((__float_as_uint(m) >> 23) & 255) - 127;
+  const int e = exp_of(m);
   return e >= -6 && e < 12 ? 0 : max(e - 4, -120);
+}
+
+// The same for 32 tokens of keys or values: none in [2^-6, 2^14), else one that brings m to the near end of
+// that range. Groups of like size then have like exponents on either side of an end: where a group's
+// exponent is below its neighbours', its softmax weights take the difference (weigh), and lose bits to it
+// once it is a good deal more than the 2^7 that they have in hand.
+__device__ __forceinline__ int group_exp(float m) {
+  const int e = exp_of(m);
+  return max(e < -6 ? e + 6 : e >= 14 ? e - 13 : 0, -120);
 }
 
 // the n lowest bits (none for n <= 0, all for n >= 32)
@@ -294,11 +308,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 template <int N>
@@ -799,7 +808,7 @@ struct Producer {
           m2 = abs_max2(m2, v[j][i].w);
         }
     }
-    return range_exp(warp_max(max_abs2<T>(m2, 0.0f)));
+    return group_exp(warp_max(max_abs2<T>(m2, 0.0f)));
   }
 
   // Buffered tokens and the chunk's own (t >= nc), times f.
@@ -871,7 +880,7 @@ struct Producer {
     float f = 1.0f;
     if constexpr (SC) {
       if (t0 >= nc || mixed) ex = raw_exp(t0);
-      if (t0 < nc) ex = max(ex, range_exp(compressed_max(cur, t0, row0, ne)));
+      if (t0 < nc) ex = max(ex, group_exp(compressed_max(cur, t0, row0, ne)));
     }
     if constexpr (SC) f = pow2i(-ex);
     if (t0 < nc) {
@@ -1281,24 +1290,28 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
           E = E1;
         }
         l *= fs;
-        const float ref = mref == -INFINITY ? 0.0f : mref;
+        const float ref = (mref == -INFINITY ? 0.0f : mref) - kWeightShift;
         float2 sum = make_float2(0.0f, 0.0f);
         auto weigh = [&](auto& s, int g, uint32_t at) {
           constexpr int N = sizeof(s) / 4;
           const float sc = score_scale(a.scale_log2, SC ? ek[g] + eq : eq);
+          // a group of smaller values than the accumulator's: its weights take the power of two before they are
+          // rounded, and their sum gives it back (beyond 2^-60 nothing is left of the values either way)
+          const int down = SC ? max(ev[g] - E1, -60) : 0;
+          const float rg = SC ? ref - (float)down : ref;
+          float2 part = make_float2(0.0f, 0.0f);
           uint32_t p[N / 2];
 #pragma unroll
           for (int c = 0; c < N; c += 2) {
-            float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), make_float2(sc, sc), make_float2(-ref, -ref));
+            float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), make_float2(sc, sc), make_float2(-rg, -rg));
             x = make_float2(ex2(x.x), ex2(x.y));
-            sum = add2(sum, x);
+            if constexpr (SC) part = add2(part, x);
+            else sum = add2(sum, x);
             p[c / 2] = pack_half2(x.x, x.y);
           }
-          if (SC && ev[g] != E1) {   // (a power of two, the same for all rows)
-            const float fv = pow2i(ev[g] - E1);
-            const uint32_t f2 = pack_half2(fv, fv);
-#pragma unroll
-            for (int c = 0; c < N / 2; ++c) p[c] = hmul2(p[c], f2);
+          if constexpr (SC) {
+            const float back = pow2i(-down);
+            sum = fma2(part, make_float2(back, back), sum);
           }
           tmem_st(at, p);
         };

@@ -146,11 +146,14 @@ def chunk_spread(kc, vc, rows, counts, q, kn, vn, tau, plen=None):
     value off, d = 2^-11 / sqrt(3) in the root mean square. A key's or value's channel takes four of them at
     most, each of no more than the sum `mag` of its parts (the scale's and the middle value's product, their
     sum, a further one for a flushed block's low-rank part or an outlier's): its variance is below
-    (2 d mag)^2. So a score's is (2 d tau)^2 sum_c q_c^2 mag_c^2 =: e_t^2, which moves the result by
-    p_t e_t (V_t - out); the weight's own rounding moves it by p_t d V_t. Sums over tokens add the squares."""
+    (2 d mag)^2; fp16 caches' values, which no power of two scales, are off by up to 2^-25 each time below
+    2^-14, with the variance 4 (2^-25)^2 / 3. So a score's is (2 d tau)^2 sum_c q_c^2 mag_c^2 =: e_t^2, which
+    moves the result by p_t e_t (V_t - out); the weight's own rounding moves it by p_t d V_t. Sums over tokens
+    add the squares."""
     d = 2.0 ** -11 / 3 ** 0.5
     if kc.dtype == torch.float32:
         d = 2.0 ** -24 * 128 ** 0.5   # a sum of 128 terms
+    tiny = 2.0 ** -25 / 3 ** 0.5 / d if kc.dtype == torch.float16 else 0.0   # beside mag
     Hq, H = q.shape[1], kc.c.H
     hq = Hq // H
     out = torch.zeros(q.shape, dtype=torch.float64, device=q.device)
@@ -183,9 +186,10 @@ def chunk_spread(kc, vc, rows, counts, q, kn, vn, tau, plen=None):
             l = w.sum(1, keepdim=True)
             w = torch.where(l > 0, w / l, 0.0)
             o = w @ v
-            e2 = (2 * d * tau) ** 2 * (qq.square() @ km.square().T)
+            km2, vm2 = (torch.where(live, x.square() + tiny * tiny, 0.0) for x in (km, vm))
+            e2 = (2 * d * tau) ** 2 * (qq.square() @ km2.T)
             far = (v.square().sum(1)[None] - 2 * o @ v.T + o.square().sum(1, keepdim=True)).clamp_min(0)
-            s2 = (w.square() * (e2 * far + d * d * (v.square() + 4 * vm.square()).sum(1)[None])).sum(1)
+            s2 = (w.square() * (e2 * far + d * d * (v.square() + 4 * vm2).sum(1)[None])).sum(1)
             out[at:at + n, h * hq:(h + 1) * hq] = o.view(n, hq, 128)
             var[at:at + n, h * hq:(h + 1) * hq] = s2.view(n, hq)
         at += n

@@ -1,0 +1,60 @@
+"""Chunk attention over values and queries of very different size, in every kernel: few query rows per unit, some,
+paired row tiles, tiles rebuilt ahead."""
+import math
+
+import pytest
+import torch
+
+from tests.serving_helpers import check_spread, chunk_spread
+from tests.test_gpu_serving import BF16, F16, F32, TAU, paged_pair, rnd
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import kv_cache_compression_gear_b200 as gear
+
+COUNTS = [3, 30, 60, 300]   # with four query heads: 12, 120, 240 and 1200 rows
+
+
+def pair(n, dt, k, v, pages=64, **codec):
+    """A paged pair of one sequence, keys and values [H][n][128] given."""
+    kc, vc = paged_pair(1, k.shape[0], pages, -(-n // pages) + 2, -(-n // pages) + 2, 4, dt, **codec)
+    kc.encode_rows([0], k[None].to(dt).contiguous())
+    vc.encode_rows([0], v[None].to(dt).contiguous())
+    return kc, vc
+
+
+def check(kc, vc, q, kn, vn, tau, what=""):
+    args = (kc, vc, [0], [q.shape[0]], q, kn, vn, tau)
+    ref, sigma = chunk_spread(*args)
+    check_spread(gear.chunk_attn(*args, out_dtype=F32), ref, sigma, F32, what)
+    assert gear.device_status() == 0
+
+
+def groups(H, n, sizes, seed):
+    """Values whose groups of 32 tokens have these deviations in turn."""
+    s = torch.tensor(sizes, device="cuda")[torch.arange(n, device="cuda") // 32 % len(sizes)]
+    return rnd(seed, H, n, 128, dt=F32) * s[None, :, None]
+
+
+SIZES = [(0.0035, 0.0042), (0.004, 0.0035, 0.0036), (1e-4, 1.0), (1.0, 1e-4, 0.02), (300.0, 0.01)]
+
+
+def peaked(dt, H, count, sizes, rank):
+    """The first token takes half of the attention and has no value to speak of, 8192 others share the rest: their
+    weights, 2^-13 of the first one's, are what the result is made of."""
+    n = 8192
+    top = rnd(1, 128, dt=F32)
+    k, v = rnd(2, H, n, 128, dt=F32) * 0.1, groups(H, n, sizes, 3)
+    k[:, 0], v[:, 0] = top, 0
+    kc, vc = pair(n, dt, k, v, rank=rank, buffer_rank=0)
+    q = (top * math.log(n) / TAU / top.square().sum() * (1 + 0.01 * rnd(4, count, 4 * H, 1, dt=F32))).to(dt)
+    kn, vn = rnd(5, count, H, 128, dt=F32) * 0.1, rnd(6, count, H, 128, dt=F32) * sizes[-1]
+    check(kc, vc, q, kn.to(dt), vn.to(dt), TAU, f"{dt} {sizes}")
+
+
+@pytest.mark.parametrize("count", COUNTS)
+@pytest.mark.parametrize("sizes", SIZES)
+def test_values_of_mixed_size_under_a_peaked_softmax(count, sizes):
+    for dt in [BF16] + [F16] * (max(sizes) < 2 and min(sizes) > 1e-3):
+        peaked(dt, 16, count, sizes, 4)
