@@ -88,7 +88,7 @@ constexpr uint32_t kTmO = 2 * kTile, kTmOCols = 144;        // accumulators in t
 constexpr float kWeightShift = 7.0f;                        // log2 of what weights are multiplied by
 
 struct __align__(16) TcBars {
-  int32_t ek[4][4], ev[2][4];   // exponents of the 32-token groups of a K / V tile
+  int32_t ek[4][4], ev[2][4];   // exponents of the 32-token groups of a K / V tile; ev[][3]: of the V unit's Rf
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], qfull[2], sfull[2], pfull[2], ofull[2];
   // The K unit's Rf has been staged; no softmax warp reads it any more. One phase each per staging, and
   // every warp on both sides takes part in each: a wait is never more than one phase from what it is for,
@@ -396,6 +396,8 @@ __device__ __forceinline__ float4 clip4(float4 v, int left) {
   return make_float4(v.x, left > 1 ? v.y : 0.0f, left > 2 ? v.z : 0.0f, left > 3 ? v.w : 0.0f);
 }
 
+__device__ __forceinline__ float4 scale4(float4 v, float f) { return make_float4(v.x * f, v.y * f, v.z * f, v.w * f); }
+
 // Four L entries q .. of a token (row of r_max binary16) as two half2, those past the rank zero.
 __device__ __forceinline__ uint2 l_clip(uint2 v, int left) {
   if (left < 4) {
@@ -484,7 +486,7 @@ __device__ __forceinline__ void add_blocks(uint32_t tile, int row0, int lead, in
 }
 
 // Rf of a block (128 rows of rp) into shared memory by one warp (`write`), entries past the
-// rank as zeros; the exponent that its entries are divided by in q Rf.
+// rank as zeros; the exponent that its entries are to be divided by.
 __device__ __forceinline__ int rf_to_smem(const float* g, int rp, int rank, uint32_t rf, bool write) {
   float m = 0.0f;
 #pragma unroll 4
@@ -628,8 +630,9 @@ struct Producer {
     return l0 + st * l_step + (isk ? ext_off(r, q >> 3) : tile_off<kTile>(r, 16 + (q >> 3))) + (q & 4) * 2;
   }
   // L of the group's prompt tokens (lane = token) into the extra columns, zeros for
-  // all others; f undoes the scale of the values, and of Rf for keys. Columns past
-  // the rank were cleared when the kernel began.
+  // all others; f undoes the scale of the values, and of Rf (which carries the size of the
+  // unit's values: without it L 2^-ex leaves binary16 where they are far from 1). Columns
+  // past the rank were cleared when the kernel began.
   __device__ __forceinline__ void put_l(int t0, int row0, uint2 lq, int st, float f) const {
     const int t = t0 + lane;
     const bool has = t < b0 && !padded(t);
@@ -833,8 +836,8 @@ struct Producer {
     }
   }
 
-  // Rf of the unit's prompt block into shared memory (96 threads), and the
-  // exponent that its entries are divided by in q Rf.
+  // Rf of the unit's prompt block into shared memory (96 threads), and the exponent that its
+  // entries are divided by in q Rf, or (bf16 values) when P L is multiplied by it.
   __device__ __forceinline__ void stage_rf() {
     const int rp = rpad_of(a.r_max), bar = isk ? 1 : 2;
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(96 * SETS) : "memory");   // no warp still reads the last unit's
@@ -885,7 +888,7 @@ struct Producer {
     if constexpr (SC) f = pow2i(-ex);
     if (t0 < nc) {
       dequant(cur, t0, tile, f);
-      put_l(t0, row0, cur.l, st, isk ? pow2i(er() - (SC ? ex : 0)) : f);
+      put_l(t0, row0, cur.l, st, pow2i(SC ? er() - ex : isk ? er() : 0));   // (fp16 values: L as it is)
       __syncwarp();
       if (t0 + 32 > b0 && nc > b0 && a.buffer_rank > 0) {
         const int rp = rpad_of(a.r_max);
@@ -950,6 +953,7 @@ struct Producer {
         if (SC && lane == 0) {
           if (isk) bars->ek[tile & 3][w] = ex;
           else bars->ev[st][w] = ex;
+          if (!isk && w == 0) bars->ev[st][3] = er();
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -996,7 +1000,10 @@ struct Producer {
         pg = page_of(t0 + 2 * kTile);
         const int ex = produce(cur, t0, row, 0);
         uint8_t* dst = a.img + (int64_t)x * kImgBytes;
-        if (SC && lane == 0) reinterpret_cast<int32_t*>(dst + kImgE)[(isk ? 0 : 4) + w] = ex;
+        if (SC && lane == 0) {
+          reinterpret_cast<int32_t*>(dst + kImgE)[(isk ? 0 : 4) + w] = ex;
+          if (!isk && w == 0) reinterpret_cast<int32_t*>(dst + kImgE)[7] = er();
+        }
         row = next;
         if (x + 1 < x1 && t0 + kTile < nc) load(cur, row);
         fence_proxy_async_smem();
@@ -1023,8 +1030,8 @@ struct Producer {
 // lanes write a row's 128 bytes. Lanes that each wrote their own row and read Rf from memory took 15000
 // cycles a segment: 12 ragged rows of 2-bit codes 265 us, this way 248 us (long units alike to 1 %).
 template <typename T>
-__device__ __forceinline__ void store_rows(const ChunkArgs& a, uint32_t own, uint32_t to, const float* gv, int rp, int rank,
-                                           int hv, float mul, bool real, int64_t at, bool whole) {
+__device__ __forceinline__ void store_rows(const ChunkArgs& a, uint32_t own, uint32_t to, const float* gv, float rscale, int rp,
+                                           int rank, int hv, float mul, bool real, int64_t at, bool whole) {
   const int lane = lane_id();
   const uint32_t reals = __ballot_sync(0xffffffffu, real);
 #pragma unroll 1
@@ -1032,7 +1039,8 @@ __device__ __forceinline__ void store_rows(const ChunkArgs& a, uint32_t own, uin
     uint32_t o[32];
     tmem_ld_32x32b_x32(to + c0, o);
     for (int q = 0; q < rank; q += 4) {
-      const float4 f = clip4(__ldg(reinterpret_cast<const float4*>(gv + (c0 + lane) * rp + q)), rank - q);
+      float4 f = clip4(__ldg(reinterpret_cast<const float4*>(gv + (c0 + lane) * rp + q)), rank - q);
+      if constexpr (!std::is_same<T, __half>::value) f = scale4(f, rscale);
       sts128(own + (lane * 16 + q) * 4, make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w)));
     }
     __syncwarp();
@@ -1237,6 +1245,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
     }
     float mref = -INFINITY, l = 0.0f;
     int E = -120;
+    [[maybe_unused]] int erv = 0;   // exponent that L of the values was multiplied by, for Rf to lose
     for (int jt = first; jt < n; jt += step) {
       const int tile = it + jt, t0 = (x - u.tile + jt) * kTile;
       tc_wait(bars, &bars->sfull[grp], ns & 1);
@@ -1252,6 +1261,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
         if constexpr (SC) {
           tc_wait(bars, &bars->vfull[tile & 1], (tile >> 1) & 1);
           E1 = max(max(E, ev[0]), max(ev[1], ev[2]));
+          erv = ev[3];
         }
         float m = -INFINITY;
         uint32_t held[32], mid[16];   // SPLIT: group 2 hv, and half of group 1
@@ -1364,8 +1374,9 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
       if (real && !whole && hv == 0) *reinterpret_cast<float2*>(part) = make_float2(first < n ? mref : -INFINITY, l);
       if (first < n) {
         const float* gv = a.V.rfac + unit * a.nblk_max * 128 * rp;
+        const float rscale = SC ? pow2i(-erv) : 1.0f;
         if constexpr (SPLIT) {
-          store_rows<T>(a, sb + kTcQ + grp * 32768 + hv * 16384 + wq * 4096, to, gv, rp, rank, hv, mul, real,
+          store_rows<T>(a, sb + kTcQ + grp * 32768 + hv * 16384 + wq * 4096, to, gv, rscale, rp, rank, hv, mul, real,
                         whole ? orow * 128 : prow * kPartRow + 4, whole);
         } else {
           if (rank > 0)   // its lines come together, not one after the other
@@ -1389,6 +1400,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
                 if (q + 4 > rank) rv[c] = clip4(rv[c], rank - q);
+                if constexpr (SC) rv[c] = scale4(rv[c], rscale);
                 v[c] = fmaf(__uint_as_float(wl[0]), rv[c].x, v[c]);
                 v[c] = fmaf(q + 1 < rank ? __uint_as_float(wl[1]) : 0.0f, rv[c].y, v[c]);
                 v[c] = fmaf(q + 2 < rank ? __uint_as_float(wl[2]) : 0.0f, rv[c].z, v[c]);

@@ -58,3 +58,14 @@ def peaked(dt, H, count, sizes, rank):
 def test_values_of_mixed_size_under_a_peaked_softmax(count, sizes):
     for dt in [BF16] + [F16] * (max(sizes) < 2 and min(sizes) > 1e-3):
         peaked(dt, 16, count, sizes, 4)
+
+
+@pytest.mark.parametrize("count", COUNTS)
+@pytest.mark.parametrize("sizes", [(2.0 ** 40, 2.0 ** 38), (2.0 ** -40, 2.0 ** -42), (2.0 ** -12, 2.0 ** -14), (2.0 ** 16, 2.0 ** 13)])
+def test_low_rank_values_far_from_one(count, sizes):
+    """The low-rank part of bf16 values of any size: its factors stay in binary16's range."""
+    peaked(BF16, 8, count, sizes, 4)
+    n = 1500
+    kc, vc = pair(n, BF16, rnd(1, 8, n, 128, dt=F32) * 0.3, groups(8, n, sizes, 3), bits=2, rank=8, buffer_rank=2)
+    q, kn, vn = rnd(4, count, 32, 128, dt=BF16), rnd(5, count, 8, 128, dt=BF16), rnd(6, count, 8, 128, dt=F32) * sizes[0]
+    check(kc, vc, q, kn, vn.to(BF16), TAU, "2 bits")
