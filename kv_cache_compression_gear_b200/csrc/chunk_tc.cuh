@@ -163,11 +163,13 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((min(max(e
 
 __device__ __forceinline__ int exp_of(float m) { return (int)((__float_as_uint(m) >> 23) & 255) - 127; }
 
-// Exponent of the power of two that a query or an Rf of at most `m` is divided by: none in
-// [2^-6, 2^12), else one that puts m at 2^4.
-__device__ __forceinline__ int range_exp(float m) {
+// Exponent of the power of two that what is at most `m` is divided by: none in [2^-6, 2^(top + 1)),
+// else one that puts m at 2^top. Queries and Rf meet in a product of 128 terms that is rounded to
+// binary16: 2^7 2^5 2^3 = 2^15 at most.
+constexpr int kQueryTop = 4, kRfTop = 2;
+__device__ __forceinline__ int range_exp(float m, int top) {
   const int e = exp_of(m);
-  return e >= -6 && e < 12 ? 0 : max(e - 4, -120);
+  return e >= -6 && e <= top ? 0 : max(e - top, -120);
 }
 
 // The same for 32 tokens of keys or values: none in [2^-6, 2^14), else one that brings m to the near end of
@@ -499,7 +501,7 @@ __device__ __forceinline__ int rf_to_smem(const float* g, int rp, int rank, uint
     if (write)
       sts128(rf + i * 16, make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)));
   }
-  return range_exp(warp_max(m));
+  return range_exp(warp_max(m), kRfTop);
 }
 
 // One code path for keys and values: the producers, the softmax groups and the
@@ -1189,7 +1191,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
           m = max_abs2<T>(v.x, max_abs2<T>(v.y, max_abs2<T>(v.z, max_abs2<T>(v.w, m))));
         }
         if constexpr (SPLIT) m = fmaxf(m, exchange(2, m));
-        eq = m > 0.0f ? range_exp(m) : 0;
+        eq = m > 0.0f ? range_exp(m, kQueryTop) : 0;
         const float f = copysignf(pow2i(-eq), a.scale_log2);   // a negative scale turns the query's sign instead
         if (SC || f != 1.0f) {
 #pragma unroll 2

@@ -5,8 +5,8 @@ import math
 import pytest
 import torch
 
-from tests.serving_helpers import check_spread, chunk_spread
-from tests.test_gpu_serving import BF16, F16, F32, TAU, paged_pair, rnd
+from tests.serving_helpers import check_chunk, check_spread, chunk_ref, chunk_spread
+from tests.test_gpu_serving import BF16, F16, F32, TAU, keys, paged_pair, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,32 @@ def test_low_rank_values_far_from_one(count, sizes):
     kc, vc = pair(n, BF16, rnd(1, 8, n, 128, dt=F32) * 0.3, groups(8, n, sizes, 3), bits=2, rank=8, buffer_rank=2)
     q, kn, vn = rnd(4, count, 32, 128, dt=BF16), rnd(5, count, 8, 128, dt=BF16), rnd(6, count, 8, 128, dt=F32) * sizes[0]
     check(kc, vc, q, kn, vn.to(BF16), TAU, "2 bits")
+
+
+@pytest.mark.parametrize("count", COUNTS)
+@pytest.mark.parametrize("rank", [4, 16])
+@pytest.mark.parametrize("dt", [F16, BF16])
+def test_large_queries_and_low_rank_keys(dt, rank, count):
+    """Queries of deviation 200 to 500, with a softmax scale as small: their products with the low-rank factors of
+    prompts of 1024 tokens and more stay finite, and right."""
+    for n, size, ks in ((1024, 200.0, 0.1), (1100, 500.0, 0.01), (1024, 900.0, 2.0), (6000, 900.0, 0.1), (1024, 0.002, 1.0)):
+        k = rnd(1, 2, n, 128, dt=F32) * ks
+        kc, vc = pair(n, dt, k, keys(2, 2, n, 128, dt=F32), rank=rank, buffer_rank=2)
+        q = (rnd(3, count, 8, 128, dt=F32) * size).to(dt)
+        kn, vn = rnd(4, count, 2, 128, dt=F32) * ks, rnd(5, count, 2, 128, dt=dt)
+        check(kc, vc, q, kn.to(dt), vn, TAU / size / ks, f"{n} {size} {ks}")
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+def test_queries_along_the_leading_direction(dt):
+    """A query along a column of the low-rank factor, with a norm of 20 to 40000."""
+    kc, vc = pair(2048, dt, rnd(1, 1, 2048, 128, dt=F32) * 0.05, keys(2, 1, 2048, 128, dt=F32), rank=4, buffer_rank=2)
+    u = kc.arrays()["rfac"][0, 0, 0, :, 0].float()
+    norms = torch.tensor([20.0, 400.0, 1500.0, 40000.0], device="cuda")
+    for count in COUNTS:
+        q = (u / u.norm() * norms[:, None]).expand(count, 4, 128).to(dt).contiguous()
+        for size in norms.tolist():   # a scale that suits one of them: the others pick one token or weigh all alike
+            got = gear.chunk_attn(kc, vc, [0], [count], q, None, None, 20 * TAU / size, out_dtype=F32)
+            ref, bound = chunk_ref(kc, vc, [0], [count], q, None, None, 20 * TAU / size)
+            check_chunk(got, ref, bound, F32, f"{count} {size}")
+    assert gear.device_status() == 0
