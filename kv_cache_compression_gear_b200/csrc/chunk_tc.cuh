@@ -292,6 +292,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -341,53 +346,42 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   return r;
 }
 
-// Codes to values, two channels per instruction. Codes are masked into the mantissa of
-// binary16 1024; the upper code of a pair (and later pairs of a byte) stays where it is in
-// the byte, which makes it 2^pos times as large: the scale takes the power of two back.
-// Less 1024 and the middle code m (2^(b-1)) they are exact, and
+// Codes to values, two channels per instruction. A code is masked where it lies in its byte, in
+// the mantissa of a binary16 number whose bit there is worth 1: 1024 for bits 0 on, 256 for 2, 64 for
+// 4 and 16 for 6. Less that number and the middle code m (2^(b-1)) it is exact, and
 //   value = (code - m) scale + (zero + m scale)
 // rounds scale, the middle value and the sum once each to 11 bits: relative to the group's
 // half range and its middle, not to `zero` (a code taken from 0 would lose a bit or two).
 template <int BITS>
 struct HalfCodes {
-  static constexpr int kPairs = BITS == 2 ? 2 : 1;   // pairs of channels per byte (8 bits: per two bytes)
   static constexpr uint32_t kMid = 1u << (BITS - 1);
-  uint32_t s[kPairs], z;
+  uint32_t s, z;
   __device__ __forceinline__ HalfCodes(float scale, float zero) {
     const float m = fmaf((float)kMid, scale, zero);
     z = pack_half2(m, m);
-    if constexpr (BITS == 8) s[0] = pack_half2(scale, scale);
-    if constexpr (BITS == 4) s[0] = pack_half2(scale, scale * 0.0625f);
-    if constexpr (BITS == 2) s[0] = pack_half2(scale, scale * 0.25f), s[1] = pack_half2(scale * 0.0625f, scale * 0.015625f);
+    s = pack_half2(scale, scale);
   }
-  static constexpr uint32_t half_bits(int v) {   // binary16 -(1024 + v), v < 1024
-    return 0xE400u + (uint32_t)v;
-  }
+  // binary16 whose mantissa bit `bit` is worth 1, and that number plus kMid, negative
+  static constexpr uint32_t one_at(int bit) { return (uint32_t)(25 - bit) << 10; }
+  static constexpr uint32_t less_mid(int bit) { return 0x8000u | one_at(bit) | kMid << bit; }
   // eight channels: chunk i of the lane's four
   __device__ __forceinline__ uint4 eight(const uint32_t (&code)[BITS], int i) const {
     uint32_t o[4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      uint32_t c, off, sc = s[0];
+      uint32_t c, off;
       if constexpr (BITS == 8) {
         c = __byte_perm(code[2 * i + (p >> 1)], 0x64646464u, p & 1 ? 0x4342 : 0x4140);
-        off = half_bits(kMid) | half_bits(kMid) << 16;
-      } else if constexpr (BITS == 4) {   // bytes p, 0, p, 0: code 2p below, 16 x code 2p + 1 above
-        c = (__byte_perm(code[i], 0, 0x4040 | p | p << 8) & 0x00F0000Fu) | 0x64006400u;
-        off = half_bits(kMid) | half_bits(16 * kMid) << 16;
+        off = less_mid(0) | less_mid(0) << 16;
+      } else if constexpr (BITS == 4) {   // bytes p, 0, p, 0: code 2p in bits 0 on, code 2p + 1 in bits 4 on
+        c = (__byte_perm(code[i], 0, 0x4040 | p | p << 8) & 0x00F0000Fu) | one_at(0) | one_at(4) << 16;
+        off = less_mid(0) | less_mid(4) << 16;
       } else {
-        const int byte = 2 * (i & 1) + (p >> 1);
-        const uint32_t v = __byte_perm(code[i >> 1], 0, 0x4040 | byte | byte << 8);
-        if ((p & 1) == 0) {
-          c = (v & 0x000C0003u) | 0x64006400u;
-          off = half_bits(kMid) | half_bits(4 * kMid) << 16;
-        } else {
-          c = (v & 0x00C00030u) | 0x64006400u;
-          off = half_bits(16 * kMid) | half_bits(64 * kMid) << 16;
-          sc = s[1 % kPairs];
-        }
+        const int byte = 2 * (i & 1) + (p >> 1), at = p & 1 ? 4 : 0;
+        c = (__byte_perm(code[i >> 1], 0, 0x4040 | byte | byte << 8) & (3u << at | 3u << (18 + at))) | one_at(at) | one_at(at + 2) << 16;
+        off = less_mid(at) | less_mid(at + 2) << 16;
       }
-      o[p] = hfma2(hadd2(c, off), sc, z);
+      o[p] = hfma2(hadd2(c, off), s, z);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
   }
@@ -682,10 +676,23 @@ struct Producer {
     return warp_max(m);
   }
 
+  static constexpr float kFineScale = 6.103515625e-5f;   // 2^-14
+  // Whether a scale of the group, times f, lies below binary16's normal range (0 does not): it would keep fewer than 11 bits.
+  __device__ __forceinline__ bool fine_scales(const RawTile<BITS>& r, int t0, float f) const {
+    bool fine = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x = scale_zero(r, j).x * f;
+      fine |= t0 + tsub + 8 * j < nc && x > 0.0f && x < kFineScale;
+    }
+    return __any_sync(0xffffffffu, fine);
+  }
+
   // D of the group's compressed tokens, times f. Padding, whatever it decodes to, becomes zeros.
   __device__ __forceinline__ void dequant(const RawTile<BITS>& r, int t0, uint32_t tile, float f) const {
     // rows tsub + 8 j have the same row & 7: the swizzle is the lane's own
     const uint32_t at = tile + (qd >> 1) * kTcHalf + (w * 32 + tsub) * 128, c0 = (((qd & 1) * 4) ^ (tsub & 7)) << 4;
+    const bool fine = !(KC && isk) && fine_scales(r, t0, f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int t = t0 + tsub + 8 * j;
@@ -708,11 +715,24 @@ struct Producer {
         }
       } else {
         const float2 m = scale_zero(r, j);
-        const HalfCodes<BITS> h2(live ? m.x * f : 0.0f, live ? m.y * f : 0.0f);
+        const float scale = live ? m.x * f : 0.0f, zero = live ? m.y * f : 0.0f;
+        if (fine) {
+          // 2^12 times the values in between; next to a middle of 8 and more the scale's lost bits are below a rounding
+          const float lift = scale < kFineScale && fabsf(zero) < 8.0f ? 4096.0f : 1.0f;
+          const HalfCodes<BITS> h2(scale * lift, zero * lift);
+          const uint32_t down = lift == 1.0f ? 0x3C003C00u : 0x0C000C00u;   // 1, 2^-12
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 o = h2.eight(r.code[j], i);
-          if (in) sts128(at + j * 1024 + (c0 ^ (i << 4)), o);
+          for (int i = 0; i < 4; ++i) {
+            const uint4 o = h2.eight(r.code[j], i);
+            if (in) sts128(at + j * 1024 + (c0 ^ (i << 4)), make_uint4(hmul2(o.x, down), hmul2(o.y, down), hmul2(o.z, down), hmul2(o.w, down)));
+          }
+        } else {
+          const HalfCodes<BITS> h2(scale, zero);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 o = h2.eight(r.code[j], i);
+            if (in) sts128(at + j * 1024 + (c0 ^ (i << 4)), o);
+          }
         }
       }
     }

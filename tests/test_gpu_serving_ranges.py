@@ -98,3 +98,16 @@ def test_queries_along_the_leading_direction(dt):
             ref, bound = chunk_ref(kc, vc, [0], [count], q, None, None, 20 * TAU / size)
             check_chunk(got, ref, bound, F32, f"{count} {size}")
     assert gear.device_status() == 0
+
+
+@pytest.mark.parametrize("count", COUNTS)
+@pytest.mark.parametrize("codec", [dict(bits=2, group_size=32), dict(bits=4), dict(bits=8, group_size=128),
+                                   dict(bits=4, meta_f16=True), dict(bits=4, kivi=True, buffer_len=64)])
+def test_small_values_of_fp16_caches(codec, count):
+    """Keys and values whose codes' scales lie near or below binary16's normal range lose no more than a rounding to it."""
+    for ks, vs in ((1.0, 2e-4), (2e-4, 1.0), (1.0, 3e-5), (3e-3, 3e-3)):
+        n = 700
+        kc, vc = pair(n, F16, rnd(1, 2, n, 128, dt=F32) * ks, rnd(2, 2, n, 128, dt=F32) * vs, rank=4, buffer_rank=2, **codec)
+        q = (rnd(3, count, 8, 128, dt=F32) / ks).to(F16)
+        kn, vn = rnd(4, count, 2, 128, dt=F32) * ks, rnd(5, count, 2, 128, dt=F32) * vs
+        check(kc, vc, q, kn.to(F16), vn.to(F16), TAU, f"{ks} {vs}")
