@@ -676,23 +676,22 @@ struct Producer {
     return warp_max(m);
   }
 
-  static constexpr float kFineScale = 6.103515625e-5f;   // 2^-14
-  // Whether a scale of the group, times f, lies below binary16's normal range (0 does not): it would keep fewer than 11 bits.
-  __device__ __forceinline__ bool fine_scales(const RawTile<BITS>& r, int t0, float f) const {
-    bool fine = false;
+  // Whether a scale of the group (of any of its 32 tokens' places), times f, lies below binary16's normal
+  // range, 2^-14 (0 does not): it would keep fewer than 11 bits.
+  static constexpr uint32_t kFineScale = 0x38800000u;
+  __device__ __forceinline__ bool fine_scales(const RawTile<BITS>& r, float f) const {
+    uint32_t least = ~0u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float x = scale_zero(r, j).x * f;
-      fine |= t0 + tsub + 8 * j < nc && x > 0.0f && x < kFineScale;
-    }
-    return __any_sync(0xffffffffu, fine);
+    for (int j = 0; j < 4; ++j) least = min(least, __float_as_uint(scale_zero(r, j).x * f) - 1u);
+    return __any_sync(0xffffffffu, least < kFineScale - 1u);
   }
 
   // D of the group's compressed tokens, times f. Padding, whatever it decodes to, becomes zeros.
   __device__ __forceinline__ void dequant(const RawTile<BITS>& r, int t0, uint32_t tile, float f) const {
     // rows tsub + 8 j have the same row & 7: the swizzle is the lane's own
     const uint32_t at = tile + (qd >> 1) * kTcHalf + (w * 32 + tsub) * 128, c0 = (((qd & 1) * 4) ^ (tsub & 7)) << 4;
-    const bool fine = !(KC && isk) && fine_scales(r, t0, f);
+    const bool fine = !(KC && isk) && fine_scales(r, f);
+    uint32_t lifted = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int t = t0 + tsub + 8 * j;
@@ -715,26 +714,27 @@ struct Producer {
         }
       } else {
         const float2 m = scale_zero(r, j);
-        const float scale = live ? m.x * f : 0.0f, zero = live ? m.y * f : 0.0f;
+        float scale = live ? m.x * f : 0.0f, zero = live ? m.y * f : 0.0f;
         if (fine) {
-          // 2^12 times the values in between; next to a middle of 8 and more the scale's lost bits are below a rounding
-          const float lift = scale < kFineScale && fabsf(zero) < 8.0f ? 4096.0f : 1.0f;
-          const HalfCodes<BITS> h2(scale * lift, zero * lift);
-          const uint32_t down = lift == 1.0f ? 0x3C003C00u : 0x0C000C00u;   // 1, 2^-12
+          // 2^12 times the values for now; next to a middle of 8 and more the scale's lost bits are below a rounding
+          if (scale < __uint_as_float(kFineScale) && fabsf(zero) < 8.0f) scale *= 4096.0f, zero *= 4096.0f, lifted |= 1u << j;
+        }
+        const HalfCodes<BITS> h2(scale, zero);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 o = h2.eight(r.code[j], i);
-            if (in) sts128(at + j * 1024 + (c0 ^ (i << 4)), make_uint4(hmul2(o.x, down), hmul2(o.y, down), hmul2(o.z, down), hmul2(o.w, down)));
-          }
-        } else {
-          const HalfCodes<BITS> h2(scale, zero);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 o = h2.eight(r.code[j], i);
-            if (in) sts128(at + j * 1024 + (c0 ^ (i << 4)), o);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const uint4 o = h2.eight(r.code[j], i);
+          if (in) sts128(at + j * 1024 + (c0 ^ (i << 4)), o);
         }
       }
+    }
+    if (fine) {   // rare, and so in a few instructions
+#pragma unroll 1
+      for (int n = 0; n < 16; ++n)
+        if ((lifted >> (n >> 2) & 1) && t0 + tsub + 8 * (n >> 2) < nc) {
+          const uint32_t p = at + (n >> 2) * 1024 + (c0 ^ ((n & 3) << 4)), down = 0x0C000C00u;   // 2^-12
+          const uint4 o = lds128(p);
+          sts128(p, make_uint4(hmul2(o.x, down), hmul2(o.y, down), hmul2(o.z, down), hmul2(o.w, down)));
+        }
     }
   }
   // Code of the lane's channel c (register index by selection: c is not constant).
