@@ -1281,6 +1281,7 @@ static int chunk_launch_args(const gear_cache* k, const int32_t* rows, const int
                              int64_t tok, ChunkArgs& a) {
   const int most = nrows - i0 < kChunkSeqs ? nrows - i0 : kChunkSeqs;
   int64_t tiles = 0;
+  bool rebuilt = false;   // a long chunk (more than one row block): the launch may rebuild every sequence's tiles
   int j = 0;
   for (; j < most; ++j) {
     const int b = rows[i0 + j];
@@ -1298,10 +1299,9 @@ static int chunk_launch_args(const gear_cache* k, const int32_t* rows, const int
       a.ncomp[j] = k->n_comp;
       a.nbuf[j] = k->n_buf;
     }
-    // long chunks (more than one row block): a launch's share of the tiles
-    if ((int64_t)counts[i0 + j] * a.hq > 256)
-      tiles += ((int64_t)a.ncomp[j] + a.nbuf[j] + counts[i0 + j] + kChunkTile - 1) / kChunkTile * a.H;
-    if (j > 0 && tiles > kChunkTiles) {
+    if (counts[i0 + j] > 0) tiles += ((int64_t)a.ncomp[j] + a.nbuf[j] + counts[i0 + j] + kChunkTile - 1) / kChunkTile * a.H;
+    rebuilt |= (int64_t)counts[i0 + j] * a.hq > kRowsUnit;
+    if (j > 0 && rebuilt && tiles > kChunkTiles) {
       tok -= counts[i0 + j];
       break;
     }

@@ -21,7 +21,8 @@ namespace gear {
 
 constexpr int kChunkTile = 96;     // tokens per tile (three groups of 32)
 constexpr int kChunkSeqs = 96;     // sequences per launch, at most
-constexpr int kChunkTiles = 4096;  // cached tiles per launch, unless one sequence has more (bounds the scratch of rebuilt tiles)
+constexpr int kChunkTiles = 4096;  // tiles of a launch with long chunks, all its sequences' together, unless one alone has
+                                   // more (bounds the scratch of rebuilt tiles)
 constexpr int64_t kChunkNumbers = int64_t(1) << 30;   // tile numbers per launch, at most (32-bit with the last run's end)
 constexpr int kImgBytes = 64640;   // a rebuilt tile (chunk_tc.cuh)
 constexpr int kRowsUnit = 256;     // rows of a unit of paired row tiles

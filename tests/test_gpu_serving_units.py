@@ -74,3 +74,13 @@ def test_row_blocks_of_one_tile(dt, hq):
     B, H = 16, 16
     kc, vc = ragged(H, [16] * B, dt, **LOW)
     check_rows(kc, vc, range(B), [80] * B, H * hq, H, dt, alone=(0, 7, 15))
+
+
+@pytest.mark.parametrize("at", [0, 13, 30])
+def test_one_long_chunk_among_short_rows(at):
+    """A call that is cut into launches so that the long chunk's tiles are rebuilt beside few others."""
+    prompts = [2000 - 7 * b for b in range(31)]
+    kc, vc = ragged(16, prompts, F16, **LOW)
+    counts = [1] * 31
+    counts[at] = 400
+    check_rows(kc, vc, range(31), counts, 64, 16, F16, alone=(0, at, 30))

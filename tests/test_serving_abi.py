@@ -172,3 +172,33 @@ def test_chunk_too_many_tiles_is_refused(gear):
         assert L.gear_chunk_workspace_bytes(k, v, ints(0), ints(n // 100), 1, 2, 1) > 0
         assert L.gear_chunk_attn(k, v, ints(0), ints(n), 1, A, 256, A, 256, A, 256, 2, 0.1, None, A, dtype, A, 1 << 62,
                                  None) == E.GEAR_ERR_UNSUPPORTED
+
+
+def test_chunk_scratch_beside_short_rows(gear):
+    """One long chunk, whose tiles are rebuilt ahead, in a call with many single tokens over long contexts: the
+    scratch holds the tiles of 4096 x 96 tokens and heads at most, wherever in the call the long chunk comes."""
+    L = gear.lib
+    B, H, P, ppr = 96, 8, 256, 100
+    p = gear.make_params()
+    nb = L.gear_paged_cache_bytes(ctypes.byref(p), B, H, 128, P, B * ppr, ppr, 4, 0)
+    nh = L.gear_paged_host_ints(B, ppr, B * ppr)
+    caches, hosts = [], []
+    for i in range(2):
+        c, host = gear.GearCacheStruct(), np.zeros(nh, np.int32)
+        L.gear_paged_cache_init(ctypes.byref(c), ctypes.byref(p), B, H, 128, P, B * ppr, ppr, 4, 0,
+                                ctypes.c_void_p((1 << 40) + (i << 38)), nb, ctypes.c_void_p(host.ctypes.data), nh, None)
+        host[:B], host[B:2 * B] = 21500, 1
+        host[0] = 8192
+        c.n_comp, c.n_buf, c.n_blk = 21500, 0, 1
+        caches.append(c)
+        hosts.append(host)
+    k, v = (ctypes.byref(c) for c in caches)
+    tile, parts = 64640, 148 * (2 * 256 * 132 * 4 + 32) + 512
+    for at in (0, 50, 95):
+        rows = [b for b in range(1, B)]
+        rows.insert(at, 0)
+        counts = [16384 if b == 0 else 1 for b in rows]
+        got = L.gear_chunk_workspace_bytes(k, v, ints(*rows), ints(*counts), B, 8 * H, 1)
+        assert 2048 * tile < got <= 4096 * tile + parts, (at, got)
+    # one sequence alone may need more
+    assert L.gear_chunk_workspace_bytes(k, v, ints(1), ints(40000), 1, 8 * H, 1) > 4096 * tile
