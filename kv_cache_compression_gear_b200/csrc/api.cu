@@ -1025,7 +1025,7 @@ gear_status gear_qk_norm_rope(const void* q, int64_t q_stride, int32_t Hq, const
 
 // Blocks that appending n tokens to a buffer of f flushes: a full buffer is
 // compressed when the next token arrives, so the last n_b tokens at most stay.
-static int append_blocks(int f, int n, int n_b) { return n > 0 ? (f + n - 1) / n_b : 0; }
+static int append_blocks(int f, int n, int n_b) { return n > 0 ? (int)(((int64_t)f + n - 1) / n_b) : 0; }
 
 constexpr int kStageBlocks = 64;   // blocks that one batched encode of gear_append_rope_rows takes
 

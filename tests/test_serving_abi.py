@@ -202,3 +202,17 @@ def test_chunk_scratch_beside_short_rows(gear):
         assert 2048 * tile < got <= 4096 * tile + parts, (at, got)
     # one sequence alone may need more
     assert L.gear_chunk_workspace_bytes(k, v, ints(1), ints(40000), 1, 8 * H, 1) > 4096 * tile
+
+
+def test_append_counts_near_2_31(gear):
+    """A buffer's fill and a count that pass 2^31 together are too much for the row, like any other large count."""
+    L, E = gear.lib, gear.gear
+    for dtype in (0, 2):
+        pr = Pair(gear, dtype=dtype)
+        before = [h.copy() for h in pr.host]
+        k, v = pr.refs()
+        for rows, counts in ((ints(0), ints(2 ** 31 - 1)), (ints(1, 0), ints(0, 2 ** 31 - 2)), (ints(1), ints(2 ** 31 - 19))):
+            st = L.gear_append_rope_rows(k, v, rows, counts, len(rows), A, 256, A, 256, None, 1e-6, None, None, 0, 0, 0, A,
+                                         1 << 40, None)
+            assert st == E.GEAR_ERR_CAPACITY
+        assert all(np.array_equal(a, b) for a, b in zip(before, pr.host))
