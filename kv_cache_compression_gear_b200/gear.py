@@ -536,10 +536,8 @@ def chunk_attn(kc, vc, rows, counts, q: torch.Tensor, k_new: torch.Tensor | None
     od = out_dtype or kc.dtype
     K, V = ctypes.byref(kc.c), ctypes.byref(vc.c)
     with _On(dev, stream) as on:
-        nbytes = lib.gear_chunk_workspace_bytes(K, V, rp, cp, nr, Hq, int(k_new is not None))
-        if nbytes == 0:
-            raise GearError(GEAR_ERR_INVALID_ARG, "gear_chunk_workspace_bytes")
-        w, wp, wn = on.scratch(nbytes)
+        # (0 bytes: refused, with its reason by the call itself)
+        w, wp, wn = on.scratch(lib.gear_chunk_workspace_bytes(K, V, rp, cp, nr, Hq, int(k_new is not None)))
         if out is None:
             out = torch.empty((T, Hq, 128), dtype=od, device=dev)
         assert out.is_contiguous() and out.dtype == od and out.shape == (T, Hq, 128) and out.device == dev

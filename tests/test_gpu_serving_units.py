@@ -84,3 +84,17 @@ def test_one_long_chunk_among_short_rows(at):
     counts = [1] * 31
     counts[at] = 400
     check_rows(kc, vc, range(31), counts, 64, 16, F16, alone=(0, at, 30))
+
+
+def test_refusals_name_their_reason():
+    """The status of a refused call, not only that there is one."""
+    from kv_cache_compression_gear_b200 import gear as G
+    kc, vc = ragged(2, [40, 33], F16)
+    q = rnd(1, 2, 2 * 129, 128)
+    with pytest.raises(gear.GearError) as e:   # more than 128 query heads per kv head
+        gear.chunk_attn(kc, vc, [0, 1], [1, 1], q, None, None, TAU)
+    assert e.value.status == G.GEAR_ERR_UNSUPPORTED
+    with pytest.raises(gear.GearError) as e:   # a row twice
+        gear.chunk_attn(kc, vc, [1, 1], [1, 1], q[:, :4], None, None, TAU)
+    assert e.value.status == G.GEAR_ERR_INVALID_ARG
+    assert gear.chunk_attn(kc, vc, [0, 1], [0, 0], q[:0, :4], None, None, TAU).shape == (0, 4, 128)
