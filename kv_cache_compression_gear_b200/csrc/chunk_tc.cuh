@@ -44,8 +44,7 @@
 // over 8192 tokens) stays well below what quantizing K and V to 4 bits does. Sums,
 // statistics and accumulators are binary32. A bf16 cache's values can lie outside
 // binary16's range: every 32 tokens of K and V, and every query row, carry a power of
-// two that scales them into it (2^0 in ordinary ranges). An fp16 cache's are taken as
-// they are.
+// two that scales them into it (2^0 in ordinary ranges). An fp16 cache's are halved.
 //
 // What bounds it (one B200, 1965 MHz). 16 rows x 4 tokens x 32 heads over 8192 4-bit
 // tokens (826 MB): 0.57 ms, 1.44 TB/s, bound by the producers, which issue about 1200
@@ -172,7 +171,11 @@ __device__ __forceinline__ int range_exp(float m, int top) {
   return e >= -6 && e <= top ? 0 : max(e - top, -120);
 }
 
-// The same for 32 tokens of keys or values: none in [2^-6, 2^14), else one that brings m to the near end of
+// An fp16 cache's keys and values are all taken half as large: rounded codes and outliers less their
+// low-rank part stay in range up to 65504. (Below 2^-13 that costs a bit of the little that binary16 has there.)
+constexpr int kF16Exp = 1;
+
+// bf16: the same for 32 tokens of keys or values: none in [2^-6, 2^14), else one that brings m to the near end of
 // that range. Groups of like size then have like exponents on either side of an end: where a group's
 // exponent is below its neighbours', its softmax weights take the difference (weigh), and lose bits to it
 // once it is a good deal more than the 2^7 that they have in hand.
@@ -784,7 +787,7 @@ struct Producer {
     const uint32_t tk = entry_token(e);
     // channel c of row 32 w + tk: half c / 64, 16-byte column (c / 8) ^ tk within it
     const uint32_t at = tile + w * 4096 + tk * 128 + ((c & 64) ? kTcHalf : 0u) + (((c << 1) ^ (tk << 4)) & 0x70) + ((c << 1) & 0xe);
-    if (e < ne && !(pad && padded(t0 + tk))) sts16(at, __half_as_ushort(__float2half_rn(SC ? v * f : v)));
+    if (e < ne && !(pad && padded(t0 + tk))) sts16(at, __half_as_ushort(__float2half_rn(v * f)));
   }
   __device__ __forceinline__ static float less(float v, uint2 l, float4 g, bool on) {
     const float2 la = __half22float2(*reinterpret_cast<const __half2*>(&l.x));
@@ -836,6 +839,7 @@ struct Producer {
     return group_exp(warp_max(max_abs2<T>(m2, 0.0f)));
   }
 
+  static constexpr uint32_t kHalf2 = 0x38003800u;   // 2^-kF16Exp twice
   // Buffered tokens and the chunk's own (t >= nc), times f.
   __device__ __forceinline__ void copy_raw(int t0, uint32_t tile, float f) const {
 #pragma unroll 1
@@ -850,7 +854,7 @@ struct Producer {
           for (int i = 0; i < 4; ++i) {
             const uint4 x = v[j][i];
             const uint4 o = SC ? make_uint4(to_half2<T>(x.x, f), to_half2<T>(x.y, f), to_half2<T>(x.z, f), to_half2<T>(x.w, f))
-                               : x;
+                               : make_uint4(hmul2(x.x, kHalf2), hmul2(x.y, kHalf2), hmul2(x.z, kHalf2), hmul2(x.w, kHalf2));
             sts128(tile + tile_off<kTile>(w * 32 + tk, qd * 4 + i), o);
           }
         }
@@ -902,7 +906,7 @@ struct Producer {
     const bool mixed = t0 < nc && t0 + 32 > nc;   // a group that ends in uncompressed tokens: one exponent for both
     const int ne = t0 < nc ? min(32, nc - t0) * a.k : 0;
     int ex = -120;
-    float f = 1.0f;
+    float f = 0.5f;   // 2^-kF16Exp
     if constexpr (SC) {
       if (t0 >= nc || mixed) ex = raw_exp(t0);
       if (t0 < nc) ex = max(ex, group_exp(compressed_max(cur, t0, row0, ne)));
@@ -910,7 +914,7 @@ struct Producer {
     if constexpr (SC) f = pow2i(-ex);
     if (t0 < nc) {
       dequant(cur, t0, tile, f);
-      put_l(t0, row0, cur.l, st, pow2i(SC ? er() - ex : isk ? er() : 0));   // (fp16 values: L as it is)
+      put_l(t0, row0, cur.l, st, SC || isk ? pow2i(er() - (SC ? ex : kF16Exp)) : f);   // (fp16 values: without Rf's)
       __syncwarp();
       if (t0 + 32 > b0 && nc > b0 && a.buffer_rank > 0) {
         const int rp = rpad_of(a.r_max);
@@ -1290,8 +1294,8 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
         if constexpr (SPLIT) {
           tmem_ld_32x32b_x32(ts + 64 * hv, held);
           tmem_ld_32x32b_x16(ts + 32 + 16 * hv, mid);
-          const float sc = score_scale(a.scale_log2, SC ? ek[2 * hv] + eq : eq);
-          const float sc1 = score_scale(a.scale_log2, SC ? ek[1] + eq : eq);
+          const float sc = score_scale(a.scale_log2, eq + (SC ? ek[2 * hv] : kF16Exp));
+          const float sc1 = score_scale(a.scale_log2, eq + (SC ? ek[1] : kF16Exp));
           tmem_ld_wait();
           if (!open) {
             hide(held, seen_bits(t0 + 64 * hv, limit, plen, b0));
@@ -1305,7 +1309,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
 #pragma unroll 1
           for (int g = 0; g < 3; ++g) {
             tmem_ld_32x32b_x32(ts + 32 * g, held);
-            const float sc = score_scale(a.scale_log2, SC ? ek[g] + eq : eq);
+            const float sc = score_scale(a.scale_log2, eq + (SC ? ek[g] : kF16Exp));
             tmem_ld_wait();
             if (!open) hide(held, seen_bits(t0 + 32 * g, limit, plen, b0));
             m = fmaxf(m, max_of(held) * sc);
@@ -1326,7 +1330,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
         float2 sum = make_float2(0.0f, 0.0f);
         auto weigh = [&](auto& s, int g, uint32_t at) {
           constexpr int N = sizeof(s) / 4;
-          const float sc = score_scale(a.scale_log2, SC ? ek[g] + eq : eq);
+          const float sc = score_scale(a.scale_log2, eq + (SC ? ek[g] : kF16Exp));
           // a group of smaller values than the accumulator's: its weights take the power of two before they are
           // rounded, and their sum gives it back (beyond 2^-60 nothing is left of the values either way)
           const int down = SC ? max(ev[g] - E1, -60) : 0;
@@ -1391,7 +1395,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, TcBars* bars, u
                                       : (orow - (int64_t)a.tok0[0] * a.Hq) * a.slots + ((int)blockIdx.x - u.tile / a.seg) * 2 + grp;
       float* part = a.part + prow * kPartRow;
       if constexpr (SPLIT) l += exchange(3, l);
-      const float up = SC ? pow2i(E) : 1.0f;
+      const float up = pow2i(SC ? E : kF16Exp);
       const float mul = whole ? (l > 0.0f ? up * __fdividef(1.0f, l) : (l == 0.0f ? 0.0f : l)) : up;
       if (real && !whole && hv == 0) *reinterpret_cast<float2*>(part) = make_float2(first < n ? mref : -INFINITY, l);
       if (first < n) {

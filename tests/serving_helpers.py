@@ -146,14 +146,14 @@ def chunk_spread(kc, vc, rows, counts, q, kn, vn, tau, plen=None):
     value off, d = 2^-11 / sqrt(3) in the root mean square. A key's or value's channel takes four of them at
     most, each of no more than the sum `mag` of its parts (the scale's and the middle value's product, their
     sum, a further one for a flushed block's low-rank part or an outlier's): its variance is below
-    (2 d mag)^2; fp16 caches' values, which no power of two scales, are off by up to 2^-25 each time below
-    2^-14, with the variance 4 (2^-25)^2 / 3. So a score's is (2 d tau)^2 sum_c q_c^2 mag_c^2 =: e_t^2, which
+    (2 d mag)^2; fp16 caches' values, which no power of two of their own scales, are held halved in binary16,
+    whose step below 2^-14 is 2^-24: half of it, doubled again, is 2^-24 each time, with the variance 4 (2^-24)^2 / 3. So a score's is (2 d tau)^2 sum_c q_c^2 mag_c^2 =: e_t^2, which
     moves the result by p_t e_t (V_t - out); the weight's own rounding moves it by p_t d V_t. Sums over tokens
     add the squares."""
     d = 2.0 ** -11 / 3 ** 0.5
     if kc.dtype == torch.float32:
         d = 2.0 ** -24 * 128 ** 0.5   # a sum of 128 terms
-    tiny = 2.0 ** -25 / 3 ** 0.5 / d if kc.dtype == torch.float16 else 0.0   # beside mag
+    tiny = 2.0 ** -24 / 3 ** 0.5 / d if kc.dtype == torch.float16 else 0.0   # beside mag
     Hq, H = q.shape[1], kc.c.H
     hq = Hq // H
     out = torch.zeros(q.shape, dtype=torch.float64, device=q.device)

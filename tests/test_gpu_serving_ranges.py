@@ -111,3 +111,22 @@ def test_small_values_of_fp16_caches(codec, count):
         q = (rnd(3, count, 8, 128, dt=F32) / ks).to(F16)
         kn, vn = rnd(4, count, 2, 128, dt=F32) * ks, rnd(5, count, 2, 128, dt=F32) * vs
         check(kc, vc, q, kn.to(F16), vn.to(F16), TAU, f"{ks} {vs}")
+
+
+@pytest.mark.parametrize("kivi", [False, True])
+@pytest.mark.parametrize("bits", [2, 4, 8])
+def test_values_up_to_the_end_of_fp16(bits, kivi):
+    """Keys or values up to 65504, of which whole tokens lie there: compressed, buffered and the chunk's own."""
+    codec = dict(bits=bits, kivi=kivi, buffer_len=64) if kivi else dict(bits=bits)
+    for top in (20000.0, 60000.0, 65504.0):
+        for big in ("keys", "values"):
+            k, v = (((rnd(i, 2, 700, 128, dt=F32) / 3).clamp(-1, 1) * top if big == name else rnd(i, 2, 700, 128, dt=F32))
+                    for i, name in ((1, "keys"), (2, "values")))
+            k[:, 40], v[:, 50] = k[:, 40].sign() * k.abs().amax(), v[:, 50].sign() * v.abs().amax()
+            kc, vc = pair(700, F16, k, v, rank=4, buffer_rank=2, **codec)
+            new = [x[:, 30:60].transpose(0, 1).to(F16).contiguous() for x in (k, v)]
+            gear.append_rope_rows(kc, vc, [0], [30], *new)
+            for count in COUNTS:
+                q = (rnd(3, count, 8, 128, dt=F32) / (top if big == "keys" else 1)).to(F16)
+                kn, vn = (x[:, :count].transpose(0, 1).to(F16).contiguous() for x in (k, v))
+                check(kc, vc, q, kn, vn, TAU, f"{top} {big} {count}")
