@@ -467,9 +467,17 @@ size_t gear_chunk_workspace_bytes(const gear_cache* k, const gear_cache* v, cons
  *              GEAR_F32; does not overlap what is read. A query that sees
  *              no token gets 0; a NaN in a query makes its own row NaN.
  * Sums, softmax and accumulators are binary32. 16-bit caches take products on
- * the tensor cores from binary16 operands: reconstructed keys and values and the
- * softmax weights are rounded to binary16 (bf16 caches' values scaled by powers
- * of two into its range); fp32 caches are binary32 throughout.
+ * the tensor cores from binary16 operands, whatever out_dtype is: reconstructed
+ * keys and values (three roundings: scale, middle value and sum of a code; one
+ * more for an outlier's slot and for a flushed block's low-rank part) and the
+ * softmax weights. The result is about 1e-3 of its norm off, where
+ * gear_decode_attn is binary32. fp16 caches' values are held halved: below 2^-13
+ * they keep fewer than 11 bits. bf16 caches' are scaled by a power of two per 32
+ * tokens and head: a value keeps its bits down to 2^-11 of the largest of them
+ * (tokens of the chunk that a query does not see included) and loses them
+ * gradually below; where the largest is below 2^-6 by 2^-j more than elsewhere in
+ * the row, weights keep theirs down to 2^(j - 21) of the row's largest.
+ * fp32 caches are binary32 throughout.
  * Errors: INVALID_ARG, UNSUPPORTED (more than 128 query heads per kv head, more
  * than 2^30 query rows in all, or a sequence of more than 2^30 products of 96 tokens with
  * a block of query rows: millions of new tokens), WORKSPACE, CUDA. */

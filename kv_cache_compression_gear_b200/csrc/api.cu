@@ -1357,7 +1357,6 @@ gear_status gear_chunk_attn(const gear_cache* k, const gear_cache* v, const int3
   a.vs = v_stride;
   a.plen = prefill_len;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
-  a.one_bits = 0x3F800000u;
   a.out = out;
   a.out_dtype = out_dtype;
   a.part = reinterpret_cast<float*>(workspace);

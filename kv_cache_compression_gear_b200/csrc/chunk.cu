@@ -246,9 +246,9 @@ __global__ void __launch_bounds__(256) chunk_join(const __grid_constant__ ChunkA
 }
 
 // What a unit costs beside its tiles (its queries, its rows of the result), in tiles. Two
-// chunks of 4096 tokens, half of whose units are short, take 553 us at 2, 504 at 4, 490 at 6, 503
-// at 8; 12 ragged chunks of up to 333 tokens 262, 259, 252, 249; 4 rows x 8 tokens over 32768
-// 190, 187, 184, 179.
+// chunks of 4096 tokens, half of whose units are short, take 525 us at 2, 484 at 4, 467 at 6, 480
+// at 8, 493 at 12; 12 ragged chunks of up to 333 tokens 257, 253, 247, 246, 248; 4 rows x 8 tokens
+// over 32768 193, 189, 186, 183, 185; 2048 tokens over 8192 430, 427, 428, 431, 436.
 constexpr int kUnitPad = 8;
 
 bool chunk_plan(ChunkArgs& a, int num_sms) {
@@ -262,8 +262,8 @@ bool chunk_plan(ChunkArgs& a, int num_sms) {
     int most_rows = 0;
     for (int i = 0; i < a.nseq; ++i) most_rows = a.n[i] * a.hq > most_rows ? a.n[i] * a.hq : most_rows;
     // One row tile: both softmax groups on it, alternate tiles. (At 128 rows the two are alike: 8
-    // sequences x 32 tokens x 4 query heads over 8192 take 140 us, as half of a pair 138 us.) Up to
-    // 32 rows more warps rebuild: 8 x 8 tokens 91 us, else 129 us.
+    // sequences x 32 tokens x 4 query heads over 8192 take 143 us, as half of a pair 141 us.) Up to
+    // 32 rows more warps rebuild: 8 x 8 tokens 89 us, else 133 us.
     a.par = most_rows <= 128 ? 2 : 1;
     a.R = a.par == 2 ? 128 : kRowsUnit;
     a.small = most_rows <= 32;
@@ -288,9 +288,11 @@ bool chunk_plan(ChunkArgs& a, int num_sms) {
   const int x = (int)x64;
   a.tile0[a.nseq] = x;
   a.sms = num_sms;
-  // Rebuild tiles ahead where they are read four times or more: 8 sequences x 192 tokens x 4
-  // query heads (three row blocks) over 8 x 4096 tokens take 267 us so and 265 us fused, 2 x 512
-  // tokens (eight) 180 us and 201 us, 8 x 100 tokens (two) 205 us and 187 us.
+  // Rebuild tiles ahead where they are read four times or more. 8 sequences over 4096 bf16 tokens x 8
+  // heads, rebuilt and fused: two row blocks each 184 and 191 us, three 235 and 270, four 282 and 356,
+  // eight 478 and 694; one sequence over 8192 71 and 74, 80 and 89, 91 and 104; 32 fp16 heads over
+  // 4096 179 and 178, 230 and 257, 279 and 337. Below four the gain is a seventh at most, for 64 KB
+  // of scratch per 96 tokens and head.
   int d = 0;
   for (int i = 0; i < a.nseq; ++i) {
     a.img0[i] = d;

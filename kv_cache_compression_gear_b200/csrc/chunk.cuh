@@ -40,7 +40,6 @@ struct ChunkArgs {
   const int32_t* table;      // null: contiguous
   const int32_t* plen;       // [B] or null: real tokens at the head of block 0
   float scale_log2;
-  uint32_t one_bits;         // 0x3F800000 (1.0f), passed so that it stays in a register
   const void* q;             // token t, head j at q + t * qs + j * 128
   const void* kn;            // null: the chunk has no keys of its own
   const void* vn;

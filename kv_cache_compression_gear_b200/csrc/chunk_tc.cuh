@@ -24,7 +24,7 @@
 // are rebuilt once, as they will lie in shared memory, and fetched by bulk copies.
 // The softmax groups then have the SM's issue slots and instruction caches to
 // themselves, and two warps share 32 rows, half of a tile's columns each (one warp
-// per 32 rows: 2 chunks of 4096 tokens 540 us, two 500 us).
+// per 32 rows: 2 chunks of 4096 tokens 540 us, two 500 us when that was built, 484 us now).
 //
 // The low-rank part of prompt tokens is not rebuilt per element: with K = D + L Rf^T,
 // q K^T = q D^T + (q Rf) L^T takes 16 more columns of the inner dimension, and
@@ -38,20 +38,22 @@
 // 2^8, so that the accumulator in tensor memory is rarely rescaled. Weights are
 // 2^7 times the formula's (their sum too): with 2^8 above the reference they stay
 // below 2^15, and down to 2^-21 of it they keep binary16's 11 bits. Rounding to
-// binary16 happens to K and V (to the scale, the middle value and the sum of a code;
-// 11 bits against the codes' 2 to 8), to q Rf and L, and to the weights: the tensor
-// cores take no wider operands at this rate, and an output's error (1e-3 of its norm
-// over 8192 tokens) stays well below what quantizing K and V to 4 bits does. Sums,
-// statistics and accumulators are binary32. A bf16 cache's values can lie outside
+// binary16 happens to K and V (to the scale, the middle value and the sum of a code: twice
+// the error of one rounding; to an outlier less its low-rank part; for flushed blocks
+// after every four ranks), to q Rf and L, and to the weights (their sum takes them
+// unrounded): the tensor cores take no wider operands at this rate, and an output's error
+// (0.7e-3 to 1.1e-3 of its norm, where rounding a binary32 result alone gives 0.2e-3) stays
+// well below what quantizing K and V to 4 bits does. Sums, statistics and accumulators are
+// binary32. A bf16 cache's values can lie outside
 // binary16's range: every 32 tokens of K and V, and every query row, carry a power of
 // two that scales them into it (2^0 in ordinary ranges). An fp16 cache's are halved.
 //
 // What bounds it (one B200, 1965 MHz). 16 rows x 4 tokens x 32 heads over 8192 4-bit
-// tokens (826 MB): 0.57 ms, 1.44 TB/s, bound by the producers, which issue about 1200
+// tokens (826 MB): 0.57 ms, 1.46 TB/s, bound by the producers, which issue about 1250
 // instructions per 32 tokens and tensor at 0.5 per cycle and scheduler; their code
 // is kept small because with straight-line copies for keys and values a tile took five
 // times as long in instruction fetches. 2048 tokens x 32 heads over 8192 (311 GFLOP):
-// 0.46 ms, 675 TFLOP/s: 3500 cycles a tile of 2 x 128 rows, of which the products take
+// 0.45 ms, 690 TFLOP/s: about 3500 cycles a tile of 2 x 128 rows, of which the products take
 // 2060 and the exponentials 1540 (16 lanes per cycle and SM), at the 1.7 GHz the power limit leaves.
 #pragma once
 
@@ -943,8 +945,8 @@ struct Producer {
     if (lane == 0) pu[4] = 0, pu[6] = 0;   // [6]: Rf's staged
     __syncwarp();
     const int begin = blockIdx.x * a.seg;
-  ChunkUnit u;
-  for (int x = begin; x < end;) {
+    ChunkUnit u;
+    for (int x = begin; x < end;) {
       u = x == begin ? chunk_find(a, x) : chunk_next(a, u);
       x = max(x, u.tile);
       if (x >= end) break;

@@ -10,7 +10,7 @@
 // head, eight consecutive channels each (one 16-byte load of 16-bit values), so
 // that the norm is four shuffles and a pair's other half is either in the same
 // lane (interleaved) or in the lane rot_dim / 16 away. 8192 tokens of 64 fp16 heads (273 MB)
-// take 61 us, 4.5 TB/s or 68 % of the measured copy bandwidth; one token of 40 heads 2.2 us.
+// take 60 us, 4.5 TB/s or 69 % of the measured copy bandwidth; one token of 40 heads 1.8 us.
 #include "common.cuh"
 #include "rope.cuh"
 
@@ -214,7 +214,12 @@ __global__ void __launch_bounds__(kFillRows) paged_fill(const __grid_constant__ 
 }
 
 // Four heads per half warp keep enough loads in flight for prompts; with few heads in
-// all, fewer each spread them over more warps.
+// all, fewer each spread them over more warps: kManyWarps of them for more heads each. Kernel
+// times with one, two and four heads per half warp, 64 fp16 heads: 128 tokens (2048 warps of two
+// heads each half) 3.5, 3.1, 3.4 us; 256 6.4, 4.6, 4.8; 1024 17, 12.9, 10.5; 8192 120, 80, 60. 40 heads: 16
+// tokens 2.2, 2.3, 2.8 us; 512 (2560 warps of four) 6.9, 6.3, 5.2; 1024 11.6, 9.3, 8.4. Four
+// also have to leave less than a quarter of the places without a head: 8192 tokens of 3 + 3 heads
+// (half of them) 17.9, 12.8, 15.7, of 5 + 1 heads 17.6, 17.5, 15.9.
 template <typename T>
 static void norm_rope_t(const NormRopeArgs& a, cudaStream_t st) {
   auto groups = [](int heads, int hp) { return (heads + 2 * hp - 1) / (2 * hp); };

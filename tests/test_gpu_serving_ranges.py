@@ -130,3 +130,18 @@ def test_values_up_to_the_end_of_fp16(bits, kivi):
                 q = (rnd(3, count, 8, 128, dt=F32) / (top if big == "keys" else 1)).to(F16)
                 kn, vn = (x[:, :count].transpose(0, 1).to(F16).contiguous() for x in (k, v))
                 check(kc, vc, q, kn, vn, TAU, f"{top} {big} {count}")
+
+
+@pytest.mark.parametrize("count", COUNTS)
+def test_large_values_without_weight_beside_small_ones(count):
+    """Every other 32 tokens have values 10000 times as large and next to no weight: the result is the small ones'."""
+    n, H = 4096, 8
+    top = rnd(1, 128, dt=F32)
+    k, v = rnd(2, H, n, 128, dt=F32) * 0.1, groups(H, n, (1e-4, 1.0), 3)
+    large = torch.arange(n, device="cuda") // 32 % 2 == 1
+    k[:, large] = -4 * top
+    k[:, 0], v[:, 0] = top, 0
+    for dt in (BF16, F16):
+        kc, vc = pair(n, dt, k, v, rank=0, buffer_rank=0)
+        q = (top * math.log(n) / TAU / top.square().sum() * (1 + 0.01 * rnd(4, count, 4 * H, 1, dt=F32))).to(dt)
+        check(kc, vc, q, None, None, TAU, f"{dt}")
